@@ -318,12 +318,10 @@ def prepare(case, seed):
     if op == "quantise":
         st["L"] = mx.mx_fp4_layout_init(case["rows"], case["K"], fmt)
         st["blob"] = torch.empty(st["L"].total_bytes, dtype=torch.uint8, device=DEV)
-    elif op in ("linear", "experts"):
-        w, act, scale = st.pop("w"), None, None
-        if case["fmt"] == "nv":                   # the scales that the plain form takes
-            act, scale = st["g"], _scale_of(w) if w.dim() == 2 else torch.cat([_scale_of(m) for m in w])
-        kind = layer.MicroscaledLinear if op == "linear" else layer.MicroscaledExperts
-        st["layer"] = kind(w, fmt, act_scale=act, weight_scale=scale)
+    elif op == "linear":
+        st["layer"] = layer.MicroscaledLinear(st.pop("w"), fmt, act_scale=st["g"] if case["fmt"] == "nv" else None)
+    elif op == "experts":
+        st["layer"] = layer.MicroscaledExperts(st.pop("w"), fmt, act_scale=st["g"] if case["fmt"] == "nv" else None)
     else:
         st["plan"] = mx.ExpertsPlan(mx.mx_experts_layout_init(case["T"], case["k"], case["E"]))
         if op == "route":
