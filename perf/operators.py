@@ -301,6 +301,19 @@ def _run_own(st):
     return st["layer"].forward(st["x"], st["ids"], st["wt"], out_dtype=TYPES[c["dtype"]])
 
 
+def _with_own_layer(st):
+    """A layer of the "nv" format, its weights held with the scales that the plain form takes: a layer's own
+    scale is the quotient max / 2688 rounded once, the plain form's on a GPU the product with 1 / 2688, and
+    where their last bits differ, blocks next to a tie of E4M3 get other scales."""
+    from mixed_precision_quantized_mx_b200 import binding as mx
+    from mixed_precision_quantized_mx_b200 import layer
+    w = st.pop("w")
+    kind, scale = ((layer.MicroscaledLinear, _scale_of(w)) if w.dim() == 2 else
+                   (layer.MicroscaledExperts, torch.cat([_scale_of(m) for m in w])))
+    st["layer"] = kind(w, mx.FP4_E4M3_16, act_scale=st["g"], weight_scale=scale)
+    return st
+
+
 def prepare(case, seed):
     st = _inputs(case, seed)
     st["case"] = case
@@ -312,6 +325,8 @@ def prepare(case, seed):
             order, pos, offsets = _sorted_slots(st["ids"], case["E"])
             st["pos"] = pos.reshape(case["T"], case["k"])
         return st
+    elif op in ("linear", "experts") and case["fmt"] == "nv":
+        return _with_own_layer(st)
     from mixed_precision_quantized_mx_b200 import binding as mx
     from mixed_precision_quantized_mx_b200 import layer
     fmt = {"nv": mx.FP4_E4M3_16, "mx": mx.FP4_E8M0_32}[case["fmt"]] if "fmt" in case else None
