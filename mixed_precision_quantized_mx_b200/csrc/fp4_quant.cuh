@@ -49,14 +49,21 @@ constexpr uint32_t kInfBits = 0x7F800000u;
 // fl(q + e r).  What is needed of the quotient is only the side of the seven E2M1
 // boundaries on which it lies; over all 2^23 significands of d and the x next to
 // each boundary, the corrected quotient and the IEEE division agree on that; the same
-// holds for a / (6 g) and the boundaries of E4M3.  Where a scale saturated, values beyond
+// holds for a / (6 g) and the boundaries of E4M3.  e is a multiple of the unit of q d and has to
+// stay one of 2^-149: next to the smallest boundary (1/4) that takes d >= 2^-101, and s may be 2^-9.
+// So below g = 2^-90 the whole division is done with x and g 2^32 times as large, which
+// leaves every quotient as it is (no bit is lost: s g is normal).  Where a scale saturated, values beyond
 // 16 d are brought to 16 d first: their codes are 6 either way, and x r cannot overflow.
+constexpr float kSmallScale = 0x1p-90f, kSmallUp = 0x1p32f;
 struct MatrixScale {
-    float g, g6, r6;                               // g, fl(6 g), fl(1 / fl(6 g))
+    float g, g6, r6;                               // g, fl(6 g), fl(1 / fl(6 g)), of `up` times the matrix
+    float up;
 };
 __device__ __forceinline__ MatrixScale matrix_scale(float g) {
+    const float up = g < kSmallScale ? kSmallUp : 1.0f;
+    g = __fmul_rn(g, up);
     const float g6 = __fmul_rn(6.0f, g);
-    return {g, g6, __frcp_rn(g6)};
+    return {g, g6, __frcp_rn(g6), up};
 }
 
 __device__ __forceinline__ float quick_div(float x, float d, float r) {
@@ -64,6 +71,7 @@ __device__ __forceinline__ float quick_div(float x, float d, float r) {
     return __fmaf_rn(__fmaf_rn(-q, d, x), r, q);
 }
 
+// s as its byte; d and r of values that are `up` times the block's
 __device__ __forceinline__ uint32_t scale16(uint32_t amax, const MatrixScale& m, float& d, float& r, bool& beyond) {
     if (amax >= kInfBits) {
         d = r = __uint_as_float(0x7FC00000u);
@@ -71,7 +79,7 @@ __device__ __forceinline__ uint32_t scale16(uint32_t amax, const MatrixScale& m,
         return 0x7Fu;
     }
     // beyond 1024 (6 g) the scale saturates however the quotient is rounded
-    const float a = __uint_as_float(amax);
+    const float a = __fmul_rn(__uint_as_float(amax), m.up);
     const uint32_t s = e4m3_bits(a < __fmul_rn(1024.0f, m.g6) ? quick_div(a, m.g6, m.r6) : 1024.0f);
     d = __fmul_rn(e4m3_value(s), m.g);
     r = d > 0.0f ? __frcp_rn(d) : 0.0f;
@@ -84,6 +92,10 @@ __device__ __forceinline__ uint32_t quant_block(float2 (&v)[8], uint32_t amax, c
     float d, r;
     bool beyond;
     const uint32_t s = scale16(amax, m, d, r, beyond);
+    if (m.up != 1.0f) {                            // the same for the whole matrix
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = make_float2(__fmul_rn(v[i].x, m.up), __fmul_rn(v[i].y, m.up));
+    }
     if (beyond) {
         const float lim = __fmul_rn(16.0f, d);
 #pragma unroll
