@@ -361,8 +361,8 @@ fp4_stream_kernel(const __grid_constant__ GemmArgs a) {
                     v[0] = scaled(v[0], scale);
                     store_cols<1>(a, row0 + int(rank) + i * int(nc), 1, nf, v);
                 }
-                __syncwarp();
-                if (lane < nc) mbar_arrive_cluster(mapa_shared(&S.red_free[b], lane));
+                __syncwarp();                    // the warp's reads come before other CTAs' next sums
+                if (lane < nc) arrive_release_cluster(mapa_shared(&S.red_free[b], lane));
             }
         }
     epi_done:;
