@@ -439,10 +439,14 @@ def _blob(t: torch.Tensor, name: str, nbytes: int) -> int:
     return t.data_ptr()
 
 
-def _fp4_opts(path: int, split: int, status, wait_timeout_us: int, test_stall: int):
+# options are values alone: a layer passes the same ones in every call
+_made_fp4_opts = functools.lru_cache(maxsize=256)(Fp4Opts)
+
+
+def _fp4_opts(path: int, split: int, status, wait_timeout_us: int, test_stall: int) -> Fp4Opts | None:
     if not (path or split or status is not None or wait_timeout_us or test_stall):
         return None
-    return ctypes.byref(Fp4Opts(path, split, _ptr(status), wait_timeout_us, test_stall))
+    return _made_fp4_opts(path, split, _ptr(status), wait_timeout_us, test_stall)
 
 
 def mx_fp4_layout_init(rows: int, K: int, format: int = FP4_E4M3_16, groups: int = 1) -> Fp4Layout:
@@ -511,14 +515,15 @@ def mx_fp4_linear_workspace_size(LW: Fp4Layout, M: int, path: int = 0, split: in
 
 def mx_fp4_linear(LW: Fp4Layout, wblob: torch.Tensor, X: torch.Tensor, Y: torch.Tensor,
                   workspace: torch.Tensor | None = None, gscale: torch.Tensor | None = None, path: int = 0, split: int = 0,
-                  status: torch.Tensor | None = None, stream=None) -> None:
+                  status: torch.Tensor | None = None, stream=None, wait_timeout_us: int = 0, test_stall: int = 0) -> None:
     """Y [M, LW.rows] = X W^T (see mx_fp4.h)."""
     M = X.shape[0]
     ldx, ldy = _rows(X, "X", M, LW.K), _rows(Y, "Y", M, LW.rows)
     _check(lib().mx_fp4_linear(LW, _blob(wblob, "weight blob", LW.total_bytes), X.data_ptr(), _code(X.dtype), M, ldx,
                                _vec(gscale, "gscale", 1), Y.data_ptr(), _code(Y.dtype), ldy, _ptr(workspace),
                                0 if workspace is None else workspace.nbytes,
-                               _fp4_opts(path, split, status, 0, 0), _stream(stream)), "mx_fp4_linear")
+                               _fp4_opts(path, split, status, wait_timeout_us, test_stall), _stream(stream)),
+           "mx_fp4_linear")
 
 
 # ------------------------------------------------------------------ experts
@@ -654,7 +659,8 @@ def mx_fp4_linear_sorted_workspace_size(LW: Fp4Layout, P: ExpertsLayout, path: i
 
 def mx_fp4_linear_sorted(LW: Fp4Layout, wblob: torch.Tensor, plan: ExpertsPlan, X: torch.Tensor, Y: torch.Tensor,
                          workspace: torch.Tensor | None = None, sorted: bool = False, gscale: torch.Tensor | None = None,
-                         path: int = 0, split: int = 0, status: torch.Tensor | None = None, stream=None) -> None:
+                         path: int = 0, split: int = 0, status: torch.Tensor | None = None, stream=None,
+                         wait_timeout_us: int = 0, test_stall: int = 0) -> None:
     """mx_fp4_quant_sorted and mx_fp4_gemm_sorted in one call."""
     ldx = _rows(X, "X", plan.P.n if sorted else plan.P.T, LW.K)
     ldy = _rows(Y, "Y", plan.P.n, LW.rows)
@@ -662,7 +668,8 @@ def mx_fp4_linear_sorted(LW: Fp4Layout, wblob: torch.Tensor, plan: ExpertsPlan, 
                                       X.data_ptr(), _code(X.dtype), ldx, _vec(gscale, "gscale", 1), Y.data_ptr(),
                                       _code(Y.dtype), ldy, _ptr(workspace),
                                       0 if workspace is None else workspace.nbytes,
-                                      _fp4_opts(path, split, status, 0, 0), _stream(stream)), "mx_fp4_linear_sorted")
+                                      _fp4_opts(path, split, status, wait_timeout_us, test_stall), _stream(stream)),
+           "mx_fp4_linear_sorted")
 
 
 def mx_fp4_experts_workspace_size(LW: Fp4Layout, P: ExpertsLayout, path: int = 0, split: int = 0) -> int:
@@ -674,10 +681,12 @@ def mx_fp4_experts_workspace_size(LW: Fp4Layout, P: ExpertsLayout, path: int = 0
 
 def mx_fp4_experts(LW: Fp4Layout, wblob: torch.Tensor, P: ExpertsLayout, ids: torch.Tensor, X: torch.Tensor,
                    w: torch.Tensor, Y: torch.Tensor, workspace: torch.Tensor, gscale: torch.Tensor | None = None,
-                   path: int = 0, split: int = 0, status: torch.Tensor | None = None, stream=None) -> None:
+                   path: int = 0, split: int = 0, status: torch.Tensor | None = None, stream=None,
+                   wait_timeout_us: int = 0, test_stall: int = 0) -> None:
     """Y [T, LW.rows]: the whole layer of experts (see mx_fp4.h)."""
     _check(lib().mx_fp4_experts(LW, _blob(wblob, "weight blob", LW.total_bytes), P, _vec(ids, "ids", P.n, torch.int32),
                                 X.data_ptr(), _code(X.dtype), _rows(X, "X", P.T, LW.K), _vec(gscale, "gscale", 1),
                                 _vec(w, "w", P.n), Y.data_ptr(), _code(Y.dtype), _rows(Y, "Y", P.T, LW.rows),
                                 _ptr(workspace), 0 if workspace is None else workspace.nbytes,
-                                _fp4_opts(path, split, status, 0, 0), _stream(stream)), "mx_fp4_experts")
+                                _fp4_opts(path, split, status, wait_timeout_us, test_stall), _stream(stream)),
+           "mx_fp4_experts")

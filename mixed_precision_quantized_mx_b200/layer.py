@@ -131,7 +131,26 @@ class GraphedLinear:
             self.graph.replay()
 
 
-class MicroscaledLinear:
+class _Microscaled:
+    """What the microscaled layers hold: the weights, the activations' scale, host geometry by the size of a
+    call, and the word in which the kernels report a wait that ran out."""
+
+    def _hold(self, blob: torch.Tensor, act_scale: torch.Tensor | None) -> None:
+        self.blob, self.act_scale, self._sizes = blob, act_scale, {}
+        self._status = torch.zeros(1, dtype=torch.int32, device=blob.device)
+
+    def check_status(self) -> None:
+        """Wait for the device and raise if a wait inside a kernel of this layer ran out since the last
+        check: an output of that time is then incomplete.  Graphs captured from the layer report here too."""
+        if self._status.is_cuda:
+            torch.cuda.synchronize(self._status.device)
+        st = int(self._status.item())
+        if st != 0:
+            self._status.zero_()
+            raise mx.MXError(st, type(self).__name__, "a wait inside a kernel ran out: an output is incomplete")
+
+
+class MicroscaledLinear(_Microscaled):
     """Y = X W^T with W and X in microscaled 4-bit floating point (see mx_fp4.h).
 
     format: mx.FP4_E4M3_16 (blocks of 16, E4M3 scales, one fp32 scale per matrix) or
@@ -139,7 +158,8 @@ class MicroscaledLinear:
     the weights' fp32 scale (device fp32 [1]; None takes it from W with mx_fp4_gscale) and
     act_scale the activations' (device fp32 [1], from calibration; None is 1).  Scratch comes
     from torch's allocator in each call, so calls on several streams, and graphs captured from
-    them, share none.
+    them, share none.  Waits inside the kernels are bounded: a call whose wait ran out leaves parts of
+    its output unwritten, which check_status reports.
     """
 
     def __init__(self, W: torch.Tensor, format: int = mx.FP4_E4M3_16, act_scale: torch.Tensor | None = None,
@@ -149,14 +169,14 @@ class MicroscaledLinear:
         if W.dim() != 2:
             raise ValueError(f"W has shape {tuple(W.shape)}, expected [N, K]")
         self.layout = mx.mx_fp4_layout_init(W.shape[0], W.shape[1], format)
-        self.blob, self.act_scale = _microscaled_weights(self.layout, W, weight_scale), act_scale
-        self._sizes = {}
+        self._hold(_microscaled_weights(self.layout, W, weight_scale), act_scale)
 
     @classmethod
     def from_blob(cls, blob: torch.Tensor, act_scale: torch.Tensor | None = None) -> "MicroscaledLinear":
         """Re-open a packed blob (for example one saved with torch.save)."""
         self = cls.__new__(cls)
-        self.layout, self.blob, self.act_scale, self._sizes = _reopen(blob), blob, act_scale, {}
+        self.layout = _reopen(blob)
+        self._hold(blob, act_scale)
         if self.layout.groups != 1:
             raise ValueError(f"blob holds {self.layout.groups} experts: open it with MicroscaledExperts")
         return self
@@ -183,13 +203,13 @@ class MicroscaledLinear:
         if n is None:
             n = self._sizes[M, path] = mx.mx_fp4_linear_workspace_size(L, M, path)
         ws = blob.new_empty(n) if n else None
-        mx.mx_fp4_linear(L, blob, X, out, ws, gscale=self.act_scale, path=path)
+        mx.mx_fp4_linear(L, blob, X, out, ws, gscale=self.act_scale, path=path, status=self._status)
         return out
 
     __call__ = forward
 
 
-class MicroscaledExperts:
+class MicroscaledExperts(_Microscaled):
     """A layer of E experts, each a microscaled 4-bit linear layer, with its routing.
 
     W [E, N, K]; weight_scale fp32 [E], else as MicroscaledLinear.  forward(X, ids, weights)
@@ -205,13 +225,13 @@ class MicroscaledExperts:
         if W.dim() != 3:
             raise ValueError(f"W has shape {tuple(W.shape)}, expected [E, N, K]")
         self.layout = mx.mx_fp4_layout_init(W.shape[1], W.shape[2], format, groups=W.shape[0])
-        self.blob, self.act_scale = _microscaled_weights(self.layout, W, weight_scale), act_scale
-        self._sizes = {}
+        self._hold(_microscaled_weights(self.layout, W, weight_scale), act_scale)
 
     @classmethod
     def from_blob(cls, blob: torch.Tensor, act_scale: torch.Tensor | None = None) -> "MicroscaledExperts":
         self = cls.__new__(cls)
-        self.layout, self.blob, self.act_scale, self._sizes = _reopen(blob), blob, act_scale, {}
+        self.layout = _reopen(blob)
+        self._hold(blob, act_scale)
         return self
 
     @property
@@ -246,7 +266,8 @@ class MicroscaledExperts:
             return out
         n = mx.mx_fp4_linear_sorted_workspace_size(L, P, path)
         ws = blob.new_empty(n) if n else None
-        mx.mx_fp4_linear_sorted(L, blob, plan, X, out, ws, sorted=sorted, gscale=self.act_scale, path=path)
+        mx.mx_fp4_linear_sorted(L, blob, plan, X, out, ws, sorted=sorted, gscale=self.act_scale, path=path,
+                                status=self._status)
         return out
 
     def combine(self, Ys: torch.Tensor, plan: mx.ExpertsPlan, weights: torch.Tensor, out: torch.Tensor | None = None,
@@ -270,7 +291,8 @@ class MicroscaledExperts:
             P = mx.mx_experts_layout_init(T, k, L.groups)
             self._sizes[T, k] = P, mx.mx_fp4_experts_workspace_size(L, P)
         P, n = self._sizes[T, k]
-        mx.mx_fp4_experts(L, blob, P, ids, X, weights, out, blob.new_empty(n), gscale=self.act_scale)
+        mx.mx_fp4_experts(L, blob, P, ids, X, weights, out, blob.new_empty(n), gscale=self.act_scale,
+                          status=self._status)
         return out
 
     __call__ = forward
