@@ -173,13 +173,16 @@ def _ptr(t: torch.Tensor | None) -> int | None:
     return t.data_ptr()
 
 
-# the current device's current stream, without building a Stream object
+# the current device's current stream, without building a Stream object; names of torch's own, which
+# another version may lack
 _current_device = getattr(torch._C, "_cuda_getDevice", None)
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(stream) -> int | None:
     if stream is None:
+        if _current_device is None or _current_stream is None:
+            return torch.cuda.current_stream().cuda_stream
         return _current_stream(_current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
