@@ -131,6 +131,9 @@ class GraphedLinear:
             self.graph.replay()
 
 
+KEPT_SIZES = 1024                                # sizes of calls whose host geometry a layer keeps
+
+
 class _Microscaled:
     """What the microscaled layers hold: the weights, the activations' scale, host geometry by the size of a
     call, and the word in which the kernels report a wait that ran out."""
@@ -138,6 +141,13 @@ class _Microscaled:
     def _hold(self, blob: torch.Tensor, act_scale: torch.Tensor | None) -> None:
         self.blob, self.act_scale, self._sizes = blob, act_scale, {}
         self._status = torch.zeros(1, dtype=torch.int32, device=blob.device)
+
+    def _keep(self, key, sizes):
+        """Host geometry of a call's size, worked out once; of so many sizes at most."""
+        if len(self._sizes) >= KEPT_SIZES:
+            self._sizes.clear()
+        self._sizes[key] = sizes
+        return sizes
 
     def check_status(self) -> None:
         """Wait for the device and raise if a wait inside a kernel of this layer ran out since the last
@@ -199,9 +209,9 @@ class MicroscaledLinear(_Microscaled):
             out = blob.new_empty((M, L.rows), dtype=out_dtype or X.dtype)
         if M == 0:
             return out
-        n = self._sizes.get((M, path))           # host geometry only
+        n = self._sizes.get((M, path))
         if n is None:
-            n = self._sizes[M, path] = mx.mx_fp4_linear_workspace_size(L, M, path)
+            n = self._keep((M, path), mx.mx_fp4_linear_workspace_size(L, M, path))
         ws = blob.new_empty(n) if n else None
         mx.mx_fp4_linear(L, blob, X, out, ws, gscale=self.act_scale, path=path, status=self._status)
         return out
@@ -287,10 +297,11 @@ class MicroscaledExperts(_Microscaled):
             out = blob.new_empty((T, L.rows), dtype=out_dtype or X.dtype)
         if T == 0:
             return out
-        if (T, k) not in self._sizes:            # host geometry only
+        sizes = self._sizes.get((T, k))
+        if sizes is None:
             P = mx.mx_experts_layout_init(T, k, L.groups)
-            self._sizes[T, k] = P, mx.mx_fp4_experts_workspace_size(L, P)
-        P, n = self._sizes[T, k]
+            sizes = self._keep((T, k), (P, mx.mx_fp4_experts_workspace_size(L, P)))
+        P, n = sizes
         mx.mx_fp4_experts(L, blob, P, ids, X, weights, out, blob.new_empty(n), gscale=self.act_scale,
                           status=self._status)
         return out
