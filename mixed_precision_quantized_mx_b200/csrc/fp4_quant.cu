@@ -272,7 +272,8 @@ __global__ void __launch_bounds__(kThreads)
 fp4_amax_kernel(const T* X, int64_t ldx, int64_t gsx, int rows, int K, uint32_t* amax) {
     const T* x = X + int64_t(blockIdx.y) * gsx;
     uint32_t m = 0;
-    for (int r = blockIdx.x * kWarps + (threadIdx.x >> 5); r < rows; r += gridDim.x * kWarps) {
+    // unsigned: the last step goes past the rows, of which there may be 2^31 - 128
+    for (unsigned r = blockIdx.x * kWarps + (threadIdx.x >> 5); r < unsigned(rows); r += gridDim.x * kWarps) {
         const T* row = x + int64_t(r) * ldx;
 #pragma unroll 8
         for (int c = threadIdx.x & 31; c < K; c += 32) {
