@@ -13,6 +13,8 @@
 // The row kernels move rows once: an item is one token (or slot) and a run of
 // columns, held by one warp with its loads in flight together.  All are bound by
 // HBM; a token's row is read once for all its slots.
+#include <mutex>
+
 #include "fp4.cuh"
 
 namespace mx {
@@ -369,6 +371,43 @@ bool vec_ok(const void* p, int64_t ld, int esz) {
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * esz) % 16 == 0;
 }
 
+// once per device: what the sort's kernel may take, and whether a cluster of its largest size with the most
+// shared memory can be placed (16 free SMs side by side)
+cudaError_t sort_prepare(bool* wide) {
+    static struct { bool done, wide; } known[64];
+    static std::mutex lock;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> hold(lock);
+    if (!known[dev].done) {
+        constexpr int kSmem = ((kSortWarps + kSortMaxCluster + 3) * kMaxExperts + 1) * 4;
+        e = cudaFuncSetAttribute(experts_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        if (e != cudaSuccess) return e;
+        e = cudaFuncSetAttribute(experts_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(kSortMaxCluster);
+        cfg.blockDim = dim3(kSortWarps * 32);
+        cfg.dynamicSmemBytes = kSmem;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = kSortMaxCluster;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, experts_sort_kernel, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            n = 0;
+        }
+        known[dev] = {true, n > 0};
+    }
+    *wide = known[dev].wide;
+    return cudaSuccess;
+}
+
 cudaError_t blocks_of(int64_t items, unsigned* blocks) {
     if (items > 0xFFFFFF00ll) return cudaErrorInvalidConfiguration;      // items are counted in 32 bits
     *blocks = unsigned((items + kWarps - 1) / kWarps);
@@ -377,11 +416,14 @@ cudaError_t blocks_of(int64_t items, unsigned* blocks) {
 
 }  // namespace
 
-cudaError_t launch_experts_sort(const mx_experts_layout& P, const int32_t* ids, void* plan, cudaStream_t s) {
-    // 1024 slots are one group of 32 for each warp of one CTA.  The stores of `order` scatter, and a CTA
-    // writes about a sector a cycle, so many slots go to 16 CTAs (65536 over 128 experts: 8.4 us,
-    // 10.9 with 8).
-    int nc = P.n > 16384 ? kSortMaxCluster : P.n > 4096 ? 8 : P.n > 2048 ? 4 : P.n > 1024 ? 2 : 1;
+// CTAs of the sort's cluster.  1024 slots are one group of 32 for each warp of one CTA.  The stores of
+// `order` scatter, and a CTA writes about a sector a cycle, so many slots go to 16 CTAs (65536 over 128
+// experts: 8.4 us, 10.9 with 8) where the device can place a cluster of that size, which is above the portable 8.
+int sort_ctas(int n, bool wide) {
+    return n > 16384 && wide ? kSortMaxCluster : n > 4096 ? 8 : n > 2048 ? 4 : n > 1024 ? 2 : 1;
+}
+
+cudaError_t launch_experts_sort_on(const mx_experts_layout& P, const int32_t* ids, void* plan, int ctas, cudaStream_t s) {
     int warps = (P.n + 31) / 32;
     warps = warps < 1 ? 1 : warps > kSortWarps ? kSortWarps : warps;
     SortArgs a{};
@@ -389,18 +431,17 @@ cudaError_t launch_experts_sort(const mx_experts_layout& P, const int32_t* ids, 
     a.p = plan_ptrs(P, plan);
     a.n = P.n;
     a.E = P.E;
-    const int64_t per = (int64_t(P.n) + int64_t(nc) * warps - 1) / (int64_t(nc) * warps);
+    const int64_t per = (int64_t(P.n) + int64_t(ctas) * warps - 1) / (int64_t(ctas) * warps);
     a.chunk = int((per + 31) / 32 * 32);
     a.bits = 32 - __builtin_clz(unsigned(P.E));
-    const size_t smem = (size_t(warps + nc + 3) * P.E + 1) * sizeof(int);
-    if (smem > 48 * 1024 || nc > 8) {
-        cudaError_t e = cudaFuncSetAttribute(experts_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (kSortWarps + kSortMaxCluster + 3) * kMaxExperts * 4 + 4);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(experts_sort_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-    }
-    return launch_ex(experts_sort_kernel, dim3(nc), dim3(warps * 32), smem, nc, true, s, a);
+    const size_t smem = (size_t(warps + ctas + 3) * P.E + 1) * sizeof(int);
+    return launch_ex(experts_sort_kernel, dim3(ctas), dim3(warps * 32), smem, ctas, true, s, a);
+}
+
+cudaError_t launch_experts_sort(const mx_experts_layout& P, const int32_t* ids, void* plan, cudaStream_t s) {
+    bool wide = false;
+    if (const cudaError_t e = sort_prepare(&wide); e != cudaSuccess) return e;
+    return launch_experts_sort_on(P, ids, plan, sort_ctas(P.n, wide), s);
 }
 
 cudaError_t launch_experts_gather(const mx_experts_layout& P, const void* plan, const void* X, mx_dtype dt, int H,

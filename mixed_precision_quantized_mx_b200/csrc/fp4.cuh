@@ -168,6 +168,9 @@ cudaError_t launch_fp4_gemm(const mx_fp4_layout& LW, const void* wblob, int M, c
 
 // experts.cu
 cudaError_t launch_experts_sort(const mx_experts_layout& P, const int32_t* ids, void* plan, cudaStream_t s);
+// the same by `ctas` CTAs (1, 2, 4, 8 or, where the device places such a cluster, 16); behind a first sort of the device
+cudaError_t launch_experts_sort_on(const mx_experts_layout& P, const int32_t* ids, void* plan, int ctas, cudaStream_t s);
+int sort_ctas(int n, bool wide);
 cudaError_t launch_experts_gather(const mx_experts_layout& P, const void* plan, const void* X, mx_dtype dt, int H,
                                   int64_t ldx, void* Xs, int64_t lds, cudaStream_t s);
 cudaError_t launch_experts_combine(const mx_experts_layout& P, const void* plan, const void* Ys, mx_dtype sdt, int H,
