@@ -14,8 +14,8 @@
  *
  * Conventions as in mx.h; row matrices (X, Xs, Ys, Y and their gradients) may
  * start at any element and have any row stride of at least a row.  ids, weights
- * and plans are dense.  T = 0 is a no-op everywhere but in mx_experts_sort,
- * which writes the empty plan.
+ * and plans are dense.  Rows have 1 to 2^31 - 1024 columns (MX_ERR_UNSUPPORTED above).
+ * T = 0 is a no-op everywhere but in mx_experts_sort, which writes the empty plan.
  */
 #ifndef MX_EXPERTS_H
 #define MX_EXPERTS_H

@@ -71,6 +71,13 @@ mx_status check_vector(const void* p, const char* name) {
     return MX_OK;
 }
 
+// the row kernels count the columns of a run of 1024 past the row's end in 32 bits
+mx_status check_columns(int H) {
+    if (H < 1) return api_fail(MX_ERR_INVALID_ARG, "H=%d", H);
+    if (H > 0x7FFFFFFF - 1023) return api_fail(MX_ERR_UNSUPPORTED, "H=%d above 2^31 - 1024", H);
+    return MX_OK;
+}
+
 mx_status check_gscale(const float* gscale, int format) {
     if (gscale == nullptr) return MX_OK;
     if (format == MX_FP4_E8M0_32)
@@ -367,6 +374,7 @@ mx_status mx_fp4_experts(const mx_fp4_layout* LW, const void* wblob, const mx_ex
     size_t need = 0;
     MX_TRY(mx_fp4_experts_workspace_size(LW, P, opts, &need));
     if (P->n == 0) return MX_OK;
+    MX_TRY(check_columns(LW->rows));
     MX_TRY(check_vector(ids, "ids"));
     MX_TRY(check_vector(w, "w"));
     MX_TRY(check_rows(Y, "Y", ydtype, LW->rows, ldy));
@@ -425,7 +433,7 @@ mx_status mx_experts_gather(const mx_experts_layout* P, const void* plan, const 
                             int64_t ldx, void* Xs, int64_t lds, void* stream) {
     MX_TRY(check_plan_layout(P));
     MX_TRY(check_dtype(dtype, "dtype"));
-    if (H < 1) return api_fail(MX_ERR_INVALID_ARG, "H=%d", H);
+    MX_TRY(check_columns(H));
     if (P->n == 0) return MX_OK;
     MX_TRY(check_buffer(plan, "plan"));
     MX_TRY(check_rows(X, "X", dtype, H, ldx));
@@ -438,7 +446,7 @@ mx_status mx_experts_gather_bwd(const mx_experts_layout* P, const void* plan, co
                                 int64_t lds, void* dX, int64_t ldx, void* stream) {
     MX_TRY(check_plan_layout(P));
     MX_TRY(check_dtype(dtype, "dtype"));
-    if (H < 1) return api_fail(MX_ERR_INVALID_ARG, "H=%d", H);
+    MX_TRY(check_columns(H));
     if (P->n == 0) return MX_OK;
     MX_TRY(check_buffer(plan, "plan"));
     MX_TRY(check_rows(dXs, "dXs", dtype, H, lds));
@@ -453,7 +461,7 @@ mx_status mx_experts_combine(const mx_experts_layout* P, const void* plan, const
     MX_TRY(check_plan_layout(P));
     MX_TRY(check_dtype(sdtype, "sdtype"));
     MX_TRY(check_dtype(ydtype, "ydtype"));
-    if (H < 1) return api_fail(MX_ERR_INVALID_ARG, "H=%d", H);
+    MX_TRY(check_columns(H));
     if (P->n == 0) return MX_OK;
     MX_TRY(check_buffer(plan, "plan"));
     MX_TRY(check_rows(Ys, "Ys", sdtype, H, lds));
@@ -469,7 +477,7 @@ mx_status mx_experts_combine_bwd(const mx_experts_layout* P, const void* plan, c
                                  int64_t ldds, float* dw, void* stream) {
     MX_TRY(check_plan_layout(P));
     MX_TRY(check_dtype(dtype, "dtype"));
-    if (H < 1) return api_fail(MX_ERR_INVALID_ARG, "H=%d", H);
+    MX_TRY(check_columns(H));
     if (P->n == 0) return MX_OK;
     MX_TRY(check_buffer(plan, "plan"));
     MX_TRY(check_rows(dY, "dY", dtype, H, ldy));
