@@ -57,9 +57,10 @@ struct QuantArgs {
 // tiles; token rows, each to the places of all its slots (quantised once)
 enum Rows { kMatrix, kSorted, kTokens };
 
-// CTAs an SM holds at least: 16-bit types of the 16-column format are bound by their arithmetic and
-// gain from more warps (4096 x 8192: 20.2 us with five, 21.7 with four); the others lose by it
-template <typename T, int FMT> constexpr int kQuantBlocks = sizeof(T) == 2 && FMT == MX_FP4_E4M3_16 ? 5 : 1;
+// CTAs an SM holds at least, 16-column format: 16-bit types are bound by their arithmetic and gain from
+// more warps (4096 x 8192: 17.7 us with five, 20.0 with four); fp32 fits four (26.4 us, three 29.4).  The
+// 32-column format, with less arithmetic, needs no bound.
+template <typename T, int FMT> constexpr int kQuantBlocks = FMT != MX_FP4_E4M3_16 ? 1 : sizeof(T) == 2 ? 5 : 4;
 
 __device__ __forceinline__ void begin() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
