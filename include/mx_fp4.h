@@ -79,8 +79,9 @@ typedef struct mx_fp4_opts {
     int32_t split;             /* stream path: CTAs (one cluster) that share a tile's K range,
                                   0 = auto, 1, 2, 4 or 8 */
     int32_t* status;           /* device int32 or NULL: kernel-side error code */
-    int32_t wait_timeout_us;   /* bound on every in-kernel wait (0 = 2 s); on expiry the
-                                  kernel writes MX_ERR_TIMEOUT to *status and returns */
+    int32_t wait_timeout_us;   /* bound on every in-kernel wait (0 = 2 s), in wall time, which also
+                                  runs while another process has the GPU; on expiry the kernel writes
+                                  MX_ERR_TIMEOUT to *status and returns, parts of Y unwritten */
     int32_t test_stall;        /* testing only: no copies are issued, so the waits run out
                                   (needs status) */
 } mx_fp4_opts;
@@ -177,7 +178,7 @@ mx_status mx_fp4_linear_sorted(const mx_fp4_layout* LW, const void* wblob, const
                                size_t ws_bytes, const mx_fp4_opts* opts, void* stream);
 
 /*
- * mx_fp4_experts -- a whole layer of experts in one call: mx_experts_sort of ids,
+ * mx_fp4_experts -- a layer of one projection per expert in one call: mx_experts_sort of ids,
  * mx_fp4_linear_sorted of the token rows X [T][ldx] into fp32 expert outputs, and
  * mx_experts_combine with the routing weights w into Y [T][ldy], which so is
  * rounded once.  The workspace (mx_fp4_experts_workspace_size bytes) holds the

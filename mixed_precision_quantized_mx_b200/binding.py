@@ -686,7 +686,7 @@ def mx_fp4_experts(LW: Fp4Layout, wblob: torch.Tensor, P: ExpertsLayout, ids: to
                    w: torch.Tensor, Y: torch.Tensor, workspace: torch.Tensor, gscale: torch.Tensor | None = None,
                    path: int = 0, split: int = 0, status: torch.Tensor | None = None, stream=None,
                    wait_timeout_us: int = 0, test_stall: int = 0) -> None:
-    """Y [T, LW.rows]: the whole layer of experts (see mx_fp4.h)."""
+    """Y [T, LW.rows]: sort, one projection per expert and weighted sum (see mx_fp4.h)."""
     _check(lib().mx_fp4_experts(LW, _blob(wblob, "weight blob", LW.total_bytes), P, _vec(ids, "ids", P.n, torch.int32),
                                 X.data_ptr(), _code(X.dtype), _rows(X, "X", P.T, LW.K), _vec(gscale, "gscale", 1),
                                 _vec(w, "w", P.n), Y.data_ptr(), _code(Y.dtype), _rows(Y, "Y", P.T, LW.rows),

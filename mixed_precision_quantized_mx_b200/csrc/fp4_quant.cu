@@ -22,7 +22,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
 // The row of a matrix that a warp of row group rg (of rgs per tile) takes.  32-bit divisions, and
-// none in the usual cases (64-bit ones cost the quantiser of 4096 x 8192 2.3 us of 18.4).
+// none in the usual cases (64-bit ones cost the quantiser of 4096 x 8192 2.3 us).
 struct Place {
     unsigned tile;       // of the blob
     int r;               // row in the tile

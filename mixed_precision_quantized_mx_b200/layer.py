@@ -166,7 +166,9 @@ class MicroscaledLinear(_Microscaled):
     format: mx.FP4_E4M3_16 (blocks of 16, E4M3 scales, one fp32 scale per matrix) or
     mx.FP4_E8M0_32 (blocks of 32, power-of-two scales).  For the first, weight_scale is
     the weights' fp32 scale (device fp32 [1]; None takes it from W with mx_fp4_gscale) and
-    act_scale the activations' (device fp32 [1], from calibration; None is 1).  Scratch comes
+    act_scale the activations' (device fp32 [1], from calibration).  None is 1: blocks of
+    activations below 6 * 2^-6 = 0.094 in size then get fewer bits of scale, and below
+    6 * 2^-10 = 0.006 they become zero.  Scratch comes
     from torch's allocator in each call, so calls on several streams, and graphs captured from
     them, share none.  Waits inside the kernels are bounded: a call whose wait ran out leaves parts of
     its output unwritten, which check_status reports.
@@ -220,12 +222,13 @@ class MicroscaledLinear(_Microscaled):
 
 
 class MicroscaledExperts(_Microscaled):
-    """A layer of E experts, each a microscaled 4-bit linear layer, with its routing.
+    """A layer of E experts, each one microscaled 4-bit projection, with its routing.
 
     W [E, N, K]; weight_scale fp32 [E], else as MicroscaledLinear.  forward(X, ids, weights)
-    runs the whole layer; sort, project and combine are its steps, for callers that put
-    something between them (an activation function, a second layer of experts over the same
-    plan) or need the plan for the gradients (mx_experts_combine_bwd, mx_experts_gather_bwd).
+    runs sort, projection and weighted sum in one call; sort, project and combine are its steps,
+    for callers that put something between them (an activation function, a second layer of experts
+    over the same plan: project with sorted=True) or need the plan for the gradients of the routing
+    (mx_experts_combine_bwd, mx_experts_gather_bwd; the product has none).
     """
 
     def __init__(self, W: torch.Tensor, format: int = mx.FP4_E4M3_16, act_scale: torch.Tensor | None = None,
