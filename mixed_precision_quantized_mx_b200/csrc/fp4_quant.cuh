@@ -52,10 +52,10 @@ constexpr uint32_t kInfBits = 0x7F800000u;
 // holds for a / (6 g) and the boundaries of E4M3.  e is a multiple of the unit of q d and has to
 // stay one of 2^-149: next to the smallest boundary (1/4) that takes d >= 2^-101, and s may be 2^-9.
 // So below g = 2^-90 the whole division is done with x and g 2^32 times as large, which
-// leaves every quotient as it is (no bit is lost: s g is normal).  Where a scale saturated, values beyond
-// 16 d are brought to 16 d first: their codes are 6 either way, and x r cannot overflow.
-// That is a path of its own (SMALL), since a factor in the usual one costs it registers (fp32, 4096 x
-// 8192: 26.4 to 29.4 us).
+// leaves every quotient as it is (no bit is lost: s g is normal).  That is a path of its own (SMALL),
+// since a factor in the usual one costs it registers (fp32, 4096 x 8192: 26.4 to 29.4 us).
+// Where a scale saturated, values beyond 16 d are brought to 16 d first: their codes are 6 either way, and
+// x r cannot overflow.
 constexpr float kSmallScale = 0x1p-90f, kSmallUp = 0x1p32f;
 struct MatrixScale {
     float g, g6, r6;                               // g, fl(6 g), fl(1 / fl(6 g)); of the scaled matrix if small
